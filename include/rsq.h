@@ -234,7 +234,7 @@ int w4a4_gemm_s8w(const uint8_t *codes_a, const float *scales_a, const int8_t *w
  *     k_cache, v_cache: n_blocks x n_kv x block_size x d_h int8,
  *     k_scale, v_scale: n_blocks x n_kv float32.
  * Request b's tokens lie, in order, in the blocks of row b of the block table
- * (B x max_blocks int32); token p in block table[b][p / block_size] at offset
+ * (B x max_blocks int32, or int64 for the _i64 calls); token p in block table[b][p / block_size] at offset
  * p % block_size.  A token's slot is block * block_size + offset.
  * A batch of new tokens is T rows: request b's new_len[b] tokens in rows
  * [cu_new[b], cu_new[b + 1]); rows from cu_new[B] on are padding.
@@ -267,6 +267,11 @@ int w4a4_gemm_s8w(const uint8_t *codes_a, const float *scales_a, const int8_t *w
 int kv8_plan(const int32_t *ctx_len, const int32_t *new_len, int B, int32_t *block_table, int max_blocks, int block_size,
              const int32_t *free_blocks, int n_free, const int32_t *cursor, int32_t *cursor_out, int32_t *cu_new,
              int32_t *seq_len, int32_t *positions, int64_t *slots, int64_t T, void *stream);
+
+/* The same with a block table of int64 ids, as index arithmetic often leaves them. */
+int kv8_plan_i64(const int32_t *ctx_len, const int32_t *new_len, int B, int64_t *block_table, int max_blocks, int block_size,
+                 const int32_t *free_blocks, int n_free, const int32_t *cursor, int32_t *cursor_out, int32_t *cu_new,
+                 int32_t *seq_len, int32_t *positions, int64_t *slots, int64_t T, void *stream);
 
 /* Quantises the keys and values of T rows (n_kv heads of d_h, `dtype`) into the
  * cache.  For every block and head that rows go to, with a = max |x| over these
@@ -305,6 +310,12 @@ int kv8_attention(const void *q, int64_t ldq, const int8_t *k_cache, const float
                   const float *v_scale, const int32_t *block_table, int max_blocks, const int32_t *seq_len,
                   const int32_t *cu_new, int B, float sm_scale, void *out, int64_t T, int n_heads, int n_kv, int d_h,
                   int block_size, int64_t n_blocks, int dtype, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* The same with a block table of int64 ids. */
+int kv8_attention_i64(const void *q, int64_t ldq, const int8_t *k_cache, const float *k_scale, const int8_t *v_cache,
+                      const float *v_scale, const int64_t *block_table, int max_blocks, const int32_t *seq_len,
+                      const int32_t *cu_new, int B, float sm_scale, void *out, int64_t T, int n_heads, int n_kv, int d_h,
+                      int block_size, int64_t n_blocks, int dtype, void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* Workspace bytes kv8_attention needs on the current device; 0 for an
  * unsupported shape. */

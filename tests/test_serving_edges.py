@@ -1,0 +1,93 @@
+"""The serving operators on the GPU where they can go wrong beside the sizes and masks of test_serving.py, against the
+references and tolerances of serving_ref.py."""
+import pytest
+import torch
+
+from tests import serving_ref as R
+from tests.test_serving import DEV, Case, _rsq, i32
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------------------------- int64 block tables
+
+def i64(v):
+    return torch.tensor(v, dtype=torch.int64, device=DEV)
+
+
+@pytest.mark.parametrize("size", [16, 128])
+def test_plan_of_an_int64_table(size):
+    rsq = _rsq()
+    ctx, new, width, T = [0, 5, size, 3 * size - 1, 0], [1, 2 * size, 0, 1, 3], 5, 2 * size + 9
+    table = [[700 + 10 * b + j for j in range(width)] for b in range(len(ctx))]
+    ids = list(range(40, 60))
+    want = R.plan(ctx, new, table, ids, 2, T, size)
+    t = i64(table)
+    cu, seq, pos, slots, cur = rsq.kv8_plan(i32(ctx), i32(new), t, i32(ids), i32([2]), T, size)
+    assert rsq.device_status() == 0 and t.dtype == torch.int64
+    assert (t.tolist(), cu.tolist(), seq.tolist(), pos.tolist(), slots.tolist(), cur.item()) == want
+    # the free list and the table's columns end
+    for n_free, columns in ((1, 5), (20, 2)):
+        cut = [r[:columns] for r in table]
+        want = R.plan(ctx, new, cut, ids[:n_free], 0, T, size)
+        t = i64(cut)
+        got = rsq.kv8_plan(i32(ctx), i32(new), t, i32(ids[:n_free]), i32([0]), T, size)
+        assert rsq.device_status() == 16
+        assert (t.tolist(), *(x.tolist() for x in got[:4]), got[4].item()) == want
+
+
+def test_plan_of_ids_that_no_cache_has():
+    """Ids from 2^31 - 1 on become slots that the append reports and skips; negative ones become slot -1."""
+    rsq = _rsq()
+    t = i64([[1 << 31], [(1 << 32) + 1], [1 << 62], [-1 << 40], [1]])
+    _, _, _, slots, _ = rsq.kv8_plan(i32([3] * 5), i32([1] * 5), t, i32([9]), i32([0]), 5, 16)
+    assert slots.tolist() == [((1 << 31) - 1) * 16 + 3] * 3 + [-1, 19]
+    kc = torch.zeros((2, 1, 16, 16), dtype=torch.int8, device=DEV)
+    ks = torch.zeros((2, 1), device=DEV)
+    vc, vs = kc.clone(), ks.clone()
+    x = torch.ones((5, 16), device=DEV)
+    rsq.kv8_append(x, x, slots, kc, ks, vc, vs)
+    assert rsq.device_status() == 8
+    assert kc.count_nonzero().item() == 16 and (kc[1, 0, 3] == 127).all()
+
+
+INT64_CASES = [([(100, 1), (300, 3), (0, 0)], 16, 4, 2, 64, torch.bfloat16), ([(5000, 1), (20, 2)], 64, 8, 2, 128, torch.bfloat16),
+               ([(90, 4), (7, 1)], 32, 5, 1, 128, torch.float32), ([(60, 3)], 16, 2, 1, 256, torch.float32),
+               ([(1500, 300), (0, 800), (45, 4)], 16, 4, 2, 128, torch.bfloat16),
+               ([(1500, 300), (0, 800), (45, 4)], 128, 4, 2, 64, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("lens,size,H,kv,dh,dtype", INT64_CASES)
+def test_attention_of_an_int64_table(lens, size, H, kv, dh, dtype):
+    """The same bits as with an int32 table; ids that would be valid by their low 32 bits are not."""
+    rsq = _rsq()
+    c = Case(lens, size, H, kv, dh, dtype, 17)
+    args = [x.to(DEV) for x in (c.q, c.kc, c.ks, c.vc, c.vs)]
+    lists = i32(c.seq), i32(c.cu)
+    assert torch.equal(rsq.kv8_attention(*args, i64(c.table), *lists), rsq.kv8_attention(*args, i32(c.table), *lists))
+    assert rsq.device_status() == 0
+    for b, n in enumerate(c.seq):
+        if n:
+            c.table[b][n // size // 2] = -1
+    want = rsq.kv8_attention(*args, i32(c.table), *lists)
+    assert rsq.device_status() == 8
+    for bad in ((1 << 32) + 1, 1 << 40, -1 << 33, c.n_blocks):
+        table = [[bad if j == -1 else j for j in r] for r in c.table]
+        assert torch.equal(rsq.kv8_attention(*args, i64(table), *lists), want)
+        assert rsq.device_status() == 8
+
+
+def test_tables_of_other_types_are_refused():
+    rsq = _rsq()
+    c = Case([(30, 1)], 16, 2, 1, 64, torch.bfloat16, 3)
+    args = [x.to(DEV) for x in (c.q, c.kc, c.ks, c.vc, c.vs)]
+    before = rsq.launch_count()
+    for dtype in (torch.int16, torch.float32, torch.uint8):
+        t = i32(c.table).to(dtype)
+        with pytest.raises(TypeError):
+            rsq.kv8_attention(*args, t, i32(c.seq), i32(c.cu))
+        with pytest.raises(TypeError):
+            rsq.kv8_plan(i32([0]), i32([1]), t, i32([1]), i32([0]), 1, 16)
+    with pytest.raises(ValueError):
+        rsq.kv8_attention(*args, i64(c.table).repeat(1, 2)[:, ::2], i32(c.seq), i32(c.cu))
+    assert rsq.launch_count() == before

@@ -115,15 +115,16 @@ cudaError_t launch_kron_affine_quant(const void *x, const float *P1, const float
 
 // ---- serving operators: the paged cache of 8-bit codes and 4-bit weights with group scales
 
-cudaError_t launch_kv8_plan(const int32_t *ctx_len, const int32_t *new_len, int B, int32_t *block_table, int max_blocks,
-                            int block_size, const int32_t *free_blocks, int n_free, const int32_t *cursor,
+// wide_table: the block table is int64, not int32.
+cudaError_t launch_kv8_plan(const int32_t *ctx_len, const int32_t *new_len, int B, void *block_table, bool wide_table,
+                            int max_blocks, int block_size, const int32_t *free_blocks, int n_free, const int32_t *cursor,
                             int32_t *cursor_out, int32_t *cu_new, int32_t *seq_len, int32_t *positions, int64_t *slots,
                             long long T, cudaStream_t s);
 cudaError_t launch_kv8_append(const void *k, long long ldk, const void *v, long long ldv, const int64_t *slots,
                               int8_t *k_cache, float *k_scale, int8_t *v_cache, float *v_scale, long long T, int n_kv,
                               int dh, int block_size, long long n_blocks, int dtype, cudaStream_t s);
 
-// Arguments of the attention kernels; shift = log2(block_size), width = columns of the block table.
+// Arguments of the attention kernels; shift = log2(block_size), width = columns of the block table (int64 or int32).
 struct Kv8Attention {
     const void *q;
     long long ldq;
@@ -131,7 +132,7 @@ struct Kv8Attention {
     const float *k_scale;
     const int8_t *v_cache;
     const float *v_scale;
-    const int32_t *table;
+    const void *table;
     const int32_t *seq_len;
     const int32_t *cu_new;
     void *out;
@@ -140,6 +141,7 @@ struct Kv8Attention {
     int B, n_heads, n_kv, dh, shift, width;
     long long n_blocks;
     float sm_scale;
+    bool wide_table;
 };
 // Head sizes without a tensor-core kernel, and any other (CUDA cores, float32).
 cudaError_t launch_kv8_attention_any(const Kv8Attention &p, int dtype, cudaStream_t s);

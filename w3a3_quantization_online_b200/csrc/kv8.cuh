@@ -31,6 +31,13 @@ __device__ __forceinline__ float kv8_scale(float v) {
     return fabsf(v) < __int_as_float(0x7F800000) ? v : __int_as_float(0x7FC00000);
 }
 
+// Entry i of the block table; an int64 one outside the cache reads as -1.
+__device__ __forceinline__ int kv8_block(const Kv8Attention &p, long long i) {
+    if (!p.wide_table) return static_cast<const int32_t *>(p.table)[i];
+    const long long id = static_cast<const int64_t *>(p.table)[i];
+    return id >= 0 && id < p.n_blocks ? int(id) : -1;
+}
+
 // The part of a request's state that every kernel clamps the same way: `n` new
 // rows starting at row `first` of the T token rows, `pos0` the position of the
 // first new token (negative when there are more new rows than tokens), `len`

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kGenWarps * 32) k_kv8_attention_any(const Kv8A
         bool vis = key < seen;
         long long row = 0, at = 0;                 // (block, head) of this lane's key, its first code
         if (vis) {
-            const int id = p.table[(long long)lo * p.width + (key >> p.shift)];
+            const int id = kv8_block(p, (long long)lo * p.width + (key >> p.shift));
             vis = id >= 0 && id < p.n_blocks;
             if (!vis) kv8_report(p.status, kErrKvBlock);
             else row = (long long)id * p.n_kv + kvh, at = ((row << p.shift) + (key & (S - 1))) * dh;

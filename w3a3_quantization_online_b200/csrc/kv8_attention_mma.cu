@@ -349,7 +349,7 @@ k_kv8_attention_mma(const Kv8Attention p, const Split sp) {
                 if (s && p.shift > 4) {
                     id[1] = id[0], ks[1] = ks[0], vs[1] = vs[0];
                 } else if (j0 + lane < nt && k2 < lim_max) {
-                    const int i = p.table[(long long)b * p.width + (k2 >> p.shift)];
+                    const int i = kv8_block(p, (long long)b * p.width + (k2 >> p.shift));
                     if (i >= 0 && i < p.n_blocks) {
                         id[s] = i;
                         ks[s] = p.k_scale[(long long)i * p.n_kv + h];

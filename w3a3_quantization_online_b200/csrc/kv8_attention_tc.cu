@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const Kv8Att
             bool there = false;
             auto id_at = [&](int j) -> int {                       // -2: no tokens there
                 const int key = j * 128 + (lane % NB) * W;
-                return key < it.kend ? p.table[(long long)it.b * p.width + (key >> p.shift)] : -2;
+                return key < it.kend ? kv8_block(p, (long long)it.b * p.width + (key >> p.shift)) : -2;
             };
             auto scales = [&](int id) {
                 there = id >= 0 && id < p.n_blocks;
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const Kv8Att
             // lane r < 16: the cache row of keys 8 r of a tile; the table is read a tile ahead
             auto id_at = [&](int j) -> int {
                 const int key = j * 128 + (lane & 15) * 8;
-                return key < it.kend ? p.table[(long long)it.b * p.width + (key >> p.shift)] : 0;
+                return key < it.kend ? kv8_block(p, (long long)it.b * p.width + (key >> p.shift)) : 0;
             };
             const int in_block = ((lane & 15) * 8) & ((1 << p.shift) - 1);
             long long row = 0;

@@ -22,9 +22,10 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 
+template <class Id>
 struct PlanArgs {
     const int32_t *ctx_len, *new_len;
-    int32_t *table;
+    Id *table;
     const int32_t *free_blocks;
     const int32_t *cursor;
     int32_t *cursor_out, *cu_new, *seq_len, *positions;
@@ -36,7 +37,9 @@ struct PlanArgs {
 
 __device__ __forceinline__ int clamp_i32(long long v) { return int(min(v, 2147483647ll)); }
 
-__global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(const PlanArgs p) {
+// Id: of the block table's entries.
+template <class Id>
+__global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(const PlanArgs<Id> p) {
     extern __shared__ int32_t psm[];
     int32_t *cu = psm;                    // B + 1: running sum of new tokens
     int32_t *start = psm + p.B + 1;       // B + 1: running sum of fresh blocks
@@ -120,8 +123,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(const PlanArgs p) {
             const long long col = at >> p.shift;
             pos = clamp_i32(at);
             if (col < p.width) {
-                const int id = col < had ? p.table[int64_t(lo) * p.width + col] : fresh(cursor + start[lo] + (col - had));
-                if (id >= 0) slot = (int64_t(id) << p.shift) + (at & (S - 1));
+                const Id id = col < had ? p.table[int64_t(lo) * p.width + col] : Id(fresh(cursor + start[lo] + (col - had)));
+                // no cache has a block 2^31 - 1: larger ids become slots that kv8_append reports
+                if (id >= 0) slot = (min(int64_t(id), int64_t(0x7FFFFFFF)) << p.shift) + (at & (S - 1));
             }
         }
         p.positions[t] = pos;
@@ -129,25 +133,33 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(const PlanArgs p) {
     }
 }
 
+template <class Id>
+cudaError_t launch(const PlanArgs<Id> &a, cudaStream_t s) {
+    if (!a.status) return cudaErrorInvalidDevice;
+    const long long by_rows = (a.T + kPlanThreads - 1) / kPlanThreads, by_req = (a.B + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
+    long long grid = by_rows > by_req ? by_rows : by_req;
+    if (grid > num_sms()) grid = num_sms();
+    if (grid < 1) grid = 1;
+    k_kv8_plan<Id><<<unsigned(grid), kPlanThreads, 2 * (a.B + 1) * sizeof(int32_t), s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) count_launch(1);
+    return e;
+}
+
 }  // namespace
 
-cudaError_t launch_kv8_plan(const int32_t *ctx_len, const int32_t *new_len, int B, int32_t *block_table, int max_blocks,
-                            int block_size, const int32_t *free_blocks, int n_free, const int32_t *cursor,
+cudaError_t launch_kv8_plan(const int32_t *ctx_len, const int32_t *new_len, int B, void *block_table, bool wide_table,
+                            int max_blocks, int block_size, const int32_t *free_blocks, int n_free, const int32_t *cursor,
                             int32_t *cursor_out, int32_t *cu_new, int32_t *seq_len, int32_t *positions, int64_t *slots,
                             long long T, cudaStream_t s) {
     int shift = 0;
     while ((1 << shift) < block_size) ++shift;
-    const PlanArgs a{ctx_len, new_len, block_table, free_blocks, cursor, cursor_out, cu_new, seq_len, positions, slots,
-                     device_status_word(), T, B, max_blocks, shift, n_free};
-    if (!a.status) return cudaErrorInvalidDevice;
-    const long long by_rows = (T + kPlanThreads - 1) / kPlanThreads, by_req = (B + kPlanThreads / 32 - 1) / (kPlanThreads / 32);
-    long long grid = by_rows > by_req ? by_rows : by_req;
-    if (grid > num_sms()) grid = num_sms();
-    if (grid < 1) grid = 1;
-    k_kv8_plan<<<unsigned(grid), kPlanThreads, 2 * (B + 1) * sizeof(int32_t), s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) count_launch(1);
-    return e;
+    int *status = device_status_word();
+    if (wide_table)
+        return launch(PlanArgs<int64_t>{ctx_len, new_len, static_cast<int64_t *>(block_table), free_blocks, cursor, cursor_out,
+                                        cu_new, seq_len, positions, slots, status, T, B, max_blocks, shift, n_free}, s);
+    return launch(PlanArgs<int32_t>{ctx_len, new_len, static_cast<int32_t *>(block_table), free_blocks, cursor, cursor_out,
+                                    cu_new, seq_len, positions, slots, status, T, B, max_blocks, shift, n_free}, s);
 }
 
 }  // namespace rsq

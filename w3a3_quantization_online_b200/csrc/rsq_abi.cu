@@ -196,6 +196,88 @@ bool kv8_long_chunks(int64_t T, int B, int n_heads, int n_kv) {
     return T * (n_heads / n_kv) >= rsq::kKv8TcRows && T >= 2ll * B;
 }
 
+// With a block table of Id (int32_t, int64_t).
+template <class Id>
+int kv8_plan_any(const int32_t *ctx_len, const int32_t *new_len, int B, Id *block_table, int max_blocks, int block_size,
+                 const int32_t *free_blocks, int n_free, const int32_t *cursor, int32_t *cursor_out, int32_t *cu_new,
+                 int32_t *seq_len, int32_t *positions, int64_t *slots, int64_t T, void *stream) {
+    if (B < 1 || B > 4096 || max_blocks < 1 || !kv8_block_size(block_size) || n_free < 0 || T < 0 ||
+        T > 0x7FFFFFFFll)
+        return RSQ_ERR_SHAPE;
+    if (!ctx_len || !new_len || !block_table || (n_free && !free_blocks) || !cursor || !cursor_out || !cu_new ||
+        !seq_len || (T && (!positions || !slots)))
+        return RSQ_ERR_NULL;
+    const int32_t *ptrs[] = {ctx_len, new_len, free_blocks, cursor, cursor_out, cu_new, seq_len, positions};
+    for (const int32_t *q : ptrs)
+        if (!aligned_own(q)) return RSQ_ERR_ALIGN;
+    if (!aligned_own(block_table) || !aligned_own(slots)) return RSQ_ERR_ALIGN;
+    const Span in[4] = {span(ctx_len, uint64_t(B) * 4), span(new_len, uint64_t(B) * 4),
+                        span(free_blocks, uint64_t(n_free) * 4), span(cursor, 4)};
+    const Span out[6] = {span(block_table, uint64_t(B) * max_blocks * sizeof(Id)), span(cursor_out, 4),
+                         span(cu_new, uint64_t(B + 1) * 4), span(seq_len, uint64_t(B) * 4),
+                         span(positions, uint64_t(T) * 4), span(slots, uint64_t(T) * 8)};
+    if (any_overlap(in, out)) return RSQ_ERR_ALIAS;
+    return finish(rsq::launch_kv8_plan(ctx_len, new_len, B, block_table, sizeof(Id) == 8, max_blocks, block_size, free_blocks,
+                                       n_free, cursor, cursor_out, cu_new, seq_len, positions, slots, T,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+template <class Id>
+int kv8_attention_any(const void *q, int64_t ldq, const int8_t *k_cache, const float *k_scale, const int8_t *v_cache,
+                      const float *v_scale, const Id *block_table, int max_blocks, const int32_t *seq_len,
+                      const int32_t *cu_new, int B, float sm_scale, void *out, int64_t T, int n_heads, int n_kv, int d_h,
+                      int block_size, int64_t n_blocks, int dtype, void *workspace, uint64_t workspace_bytes, void *stream) {
+    int st = kv8_check_cache(n_kv, d_h, block_size, n_blocks, dtype);
+    if (st != RSQ_OK) return st;
+    const int64_t width = int64_t(n_heads) * d_h;
+    if (!kv8_heads(n_heads, n_kv) || T < 0 || T > 0x7FFFFFFFll || B < 0 || B > 4096 || max_blocks < 1 ||
+        max_blocks > 0x7FFFFFFF / block_size || kv8_check_rows(ldq, width, dtype))
+        return RSQ_ERR_SHAPE;
+    if (!std::isfinite(sm_scale)) return RSQ_ERR_VALUE;
+    if (T == 0 || B == 0) return RSQ_OK;
+    const void *ptrs[] = {q, k_cache, k_scale, v_cache, v_scale, out, workspace};
+    const int32_t *lists[] = {seq_len, cu_new};
+    for (const void *a : ptrs)
+        if (!a) return RSQ_ERR_NULL;
+    for (const int32_t *a : lists)
+        if (!a) return RSQ_ERR_NULL;
+    if (!block_table) return RSQ_ERR_NULL;
+    for (const void *a : ptrs)
+        if (!aligned16(a)) return RSQ_ERR_ALIGN;
+    for (const int32_t *a : lists)
+        if (!aligned_own(a)) return RSQ_ERR_ALIGN;
+    if (!aligned_own(block_table)) return RSQ_ERR_ALIGN;
+    const uint64_t need = ::kv8_attention_workspace_bytes(T, B, n_heads, n_kv, d_h);
+    if (workspace_bytes < need) return RSQ_ERR_VALUE;
+    const Span in[8] = {rows_span(q, T, ldq, width, dtype),
+                        kv8_codes_span(k_cache, n_blocks, n_kv, block_size, d_h),
+                        kv8_scales_span(k_scale, n_blocks, n_kv),
+                        kv8_codes_span(v_cache, n_blocks, n_kv, block_size, d_h),
+                        kv8_scales_span(v_scale, n_blocks, n_kv),
+                        span(block_table, uint64_t(B) * max_blocks * sizeof(Id)), span(seq_len, uint64_t(B) * 4),
+                        span(cu_new, uint64_t(B + 1) * 4)};
+    const Span outs[2] = {rows_span(out, T, width, width, dtype), span(workspace, need)};
+    if (any_overlap(in, outs)) return RSQ_ERR_ALIAS;
+    int shift = 0;
+    while ((1 << shift) < block_size) ++shift;
+    rsq::Kv8Attention a{q, ldq, k_cache, k_scale, v_cache, v_scale, block_table, seq_len, cu_new, out,
+                        rsq::device_status_word(), T, B, n_heads, n_kv, d_h, shift, max_blocks, n_blocks, sm_scale,
+                        sizeof(Id) == 8};
+    if (!a.status) return finish(cudaErrorInvalidDevice);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (rsq::kv8_attention_mma_supports(d_h)) {
+        // a table too short for a long request spares its kernels' launch
+        const bool tc = dtype == RSQ_BF16 && kv8_long_chunks(T, B, n_heads, n_kv) &&
+                        T * (n_heads / n_kv) >= rsq::kKv8TcWork / (int64_t(max_blocks) * block_size);
+        if (tc) {
+            const cudaError_t e = rsq::launch_kv8_attention_tc(a, workspace, cs);
+            if (e != cudaSuccess) return finish(e);
+        }
+        return finish(rsq::launch_kv8_attention_mma(a, dtype, workspace, tc, cs));
+    }
+    return finish(rsq::launch_kv8_attention_any(a, dtype, cs));
+}
+
 }  // namespace
 
 extern "C" {
@@ -452,25 +534,15 @@ int w4a4_gemm_s8w(const uint8_t *codes_a, const float *scales_a, const int8_t *w
 int kv8_plan(const int32_t *ctx_len, const int32_t *new_len, int B, int32_t *block_table, int max_blocks, int block_size,
              const int32_t *free_blocks, int n_free, const int32_t *cursor, int32_t *cursor_out, int32_t *cu_new,
              int32_t *seq_len, int32_t *positions, int64_t *slots, int64_t T, void *stream) {
-    if (B < 1 || B > 4096 || max_blocks < 1 || !kv8_block_size(block_size) || n_free < 0 || T < 0 ||
-        T > 0x7FFFFFFFll)
-        return RSQ_ERR_SHAPE;
-    if (!ctx_len || !new_len || !block_table || (n_free && !free_blocks) || !cursor || !cursor_out || !cu_new ||
-        !seq_len || (T && (!positions || !slots)))
-        return RSQ_ERR_NULL;
-    const int32_t *ptrs[] = {ctx_len, new_len, block_table, free_blocks, cursor, cursor_out, cu_new, seq_len, positions};
-    for (const int32_t *q : ptrs)
-        if (!aligned_own(q)) return RSQ_ERR_ALIGN;
-    if (!aligned_own(slots)) return RSQ_ERR_ALIGN;
-    const Span in[4] = {span(ctx_len, uint64_t(B) * 4), span(new_len, uint64_t(B) * 4),
-                        span(free_blocks, uint64_t(n_free) * 4), span(cursor, 4)};
-    const Span out[6] = {span(block_table, uint64_t(B) * max_blocks * 4), span(cursor_out, 4),
-                         span(cu_new, uint64_t(B + 1) * 4), span(seq_len, uint64_t(B) * 4),
-                         span(positions, uint64_t(T) * 4), span(slots, uint64_t(T) * 8)};
-    if (any_overlap(in, out)) return RSQ_ERR_ALIAS;
-    return finish(rsq::launch_kv8_plan(ctx_len, new_len, B, block_table, max_blocks, block_size, free_blocks, n_free,
-                                       cursor, cursor_out, cu_new, seq_len, positions, slots, T,
-                                       static_cast<cudaStream_t>(stream)));
+    return kv8_plan_any(ctx_len, new_len, B, block_table, max_blocks, block_size, free_blocks, n_free, cursor, cursor_out,
+                        cu_new, seq_len, positions, slots, T, stream);
+}
+
+int kv8_plan_i64(const int32_t *ctx_len, const int32_t *new_len, int B, int64_t *block_table, int max_blocks, int block_size,
+                 const int32_t *free_blocks, int n_free, const int32_t *cursor, int32_t *cursor_out, int32_t *cu_new,
+                 int32_t *seq_len, int32_t *positions, int64_t *slots, int64_t T, void *stream) {
+    return kv8_plan_any(ctx_len, new_len, B, block_table, max_blocks, block_size, free_blocks, n_free, cursor, cursor_out,
+                        cu_new, seq_len, positions, slots, T, stream);
 }
 
 int kv8_append(const void *k, int64_t ldk, const void *v, int64_t ldv, const int64_t *slots, int8_t *k_cache,
@@ -512,52 +584,18 @@ int kv8_attention(const void *q, int64_t ldq, const int8_t *k_cache, const float
                   const float *v_scale, const int32_t *block_table, int max_blocks, const int32_t *seq_len,
                   const int32_t *cu_new, int B, float sm_scale, void *out, int64_t T, int n_heads, int n_kv, int d_h,
                   int block_size, int64_t n_blocks, int dtype, void *workspace, uint64_t workspace_bytes, void *stream) {
-    int st = kv8_check_cache(n_kv, d_h, block_size, n_blocks, dtype);
-    if (st != RSQ_OK) return st;
-    const int64_t width = int64_t(n_heads) * d_h;
-    if (!kv8_heads(n_heads, n_kv) || T < 0 || T > 0x7FFFFFFFll || B < 0 || B > 4096 || max_blocks < 1 ||
-        max_blocks > 0x7FFFFFFF / block_size || kv8_check_rows(ldq, width, dtype))
-        return RSQ_ERR_SHAPE;
-    if (!std::isfinite(sm_scale)) return RSQ_ERR_VALUE;
-    if (T == 0 || B == 0) return RSQ_OK;
-    const void *ptrs[] = {q, k_cache, k_scale, v_cache, v_scale, out, workspace};
-    const int32_t *lists[] = {block_table, seq_len, cu_new};
-    for (const void *a : ptrs)
-        if (!a) return RSQ_ERR_NULL;
-    for (const int32_t *a : lists)
-        if (!a) return RSQ_ERR_NULL;
-    for (const void *a : ptrs)
-        if (!aligned16(a)) return RSQ_ERR_ALIGN;
-    for (const int32_t *a : lists)
-        if (!aligned_own(a)) return RSQ_ERR_ALIGN;
-    const uint64_t need = kv8_attention_workspace_bytes(T, B, n_heads, n_kv, d_h);
-    if (workspace_bytes < need) return RSQ_ERR_VALUE;
-    const Span in[8] = {rows_span(q, T, ldq, width, dtype),
-                        kv8_codes_span(k_cache, n_blocks, n_kv, block_size, d_h),
-                        kv8_scales_span(k_scale, n_blocks, n_kv),
-                        kv8_codes_span(v_cache, n_blocks, n_kv, block_size, d_h),
-                        kv8_scales_span(v_scale, n_blocks, n_kv),
-                        span(block_table, uint64_t(B) * max_blocks * 4), span(seq_len, uint64_t(B) * 4),
-                        span(cu_new, uint64_t(B + 1) * 4)};
-    const Span outs[2] = {rows_span(out, T, width, width, dtype), span(workspace, need)};
-    if (any_overlap(in, outs)) return RSQ_ERR_ALIAS;
-    int shift = 0;
-    while ((1 << shift) < block_size) ++shift;
-    rsq::Kv8Attention a{q, ldq, k_cache, k_scale, v_cache, v_scale, block_table, seq_len, cu_new, out,
-                        rsq::device_status_word(), T, B, n_heads, n_kv, d_h, shift, max_blocks, n_blocks, sm_scale};
-    if (!a.status) return finish(cudaErrorInvalidDevice);
-    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (rsq::kv8_attention_mma_supports(d_h)) {
-        // a table too short for a long request spares its kernels' launch
-        const bool tc = dtype == RSQ_BF16 && kv8_long_chunks(T, B, n_heads, n_kv) &&
-                        T * (n_heads / n_kv) >= rsq::kKv8TcWork / (int64_t(max_blocks) * block_size);
-        if (tc) {
-            const cudaError_t e = rsq::launch_kv8_attention_tc(a, workspace, cs);
-            if (e != cudaSuccess) return finish(e);
-        }
-        return finish(rsq::launch_kv8_attention_mma(a, dtype, workspace, tc, cs));
-    }
-    return finish(rsq::launch_kv8_attention_any(a, dtype, cs));
+    return kv8_attention_any(q, ldq, k_cache, k_scale, v_cache, v_scale, block_table, max_blocks, seq_len, cu_new, B,
+                             sm_scale, out, T, n_heads, n_kv, d_h, block_size, n_blocks, dtype, workspace, workspace_bytes,
+                             stream);
+}
+
+int kv8_attention_i64(const void *q, int64_t ldq, const int8_t *k_cache, const float *k_scale, const int8_t *v_cache,
+                      const float *v_scale, const int64_t *block_table, int max_blocks, const int32_t *seq_len,
+                      const int32_t *cu_new, int B, float sm_scale, void *out, int64_t T, int n_heads, int n_kv, int d_h,
+                      int block_size, int64_t n_blocks, int dtype, void *workspace, uint64_t workspace_bytes, void *stream) {
+    return kv8_attention_any(q, ldq, k_cache, k_scale, v_cache, v_scale, block_table, max_blocks, seq_len, cu_new, B,
+                             sm_scale, out, T, n_heads, n_kv, d_h, block_size, n_blocks, dtype, workspace, workspace_bytes,
+                             stream);
 }
 
 // ---- 4-bit weights with group scales

@@ -49,11 +49,15 @@ _lib.w4a4_gemm_s8w.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _
 _lib.w4a4_gemm_s8w.restype = _i32
 _lib.kv8_plan.argtypes = [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
 _lib.kv8_plan.restype = _i32
+_lib.kv8_plan_i64.argtypes = _lib.kv8_plan.argtypes
+_lib.kv8_plan_i64.restype = _i32
 _lib.kv8_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64, _i32, _vp]
 _lib.kv8_append.restype = _i32
 _lib.kv8_attention.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _f32, _vp, _i64, _i32, _i32, _i32,
                                _i32, _i64, _i32, _vp, ctypes.c_uint64, _vp]
 _lib.kv8_attention.restype = _i32
+_lib.kv8_attention_i64.argtypes = _lib.kv8_attention.argtypes
+_lib.kv8_attention_i64.restype = _i32
 _lib.kv8_attention_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32]
 _lib.kv8_attention_workspace_bytes.restype = ctypes.c_uint64
 _lib.w4_matvec.argtypes = [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp]
@@ -81,7 +85,7 @@ _lib.rsq_selftest_wait_timeout.restype = _i32
 
 EXPORTED = ("rsq_residual_align", "rsq_align_norm_quant", "rht_quant", "rht_quant_silu_gate", "rht_heads",
             "rht_heads_quant", "rht_head_mix_quant", "kron_affine_quant", "w4a4_gemm", "w4a4_prepare_weights", "w4a4_gemm_s8w",
-            "kv8_plan", "kv8_append", "kv8_attention", "kv8_attention_workspace_bytes", "w4_matvec",
+            "kv8_plan", "kv8_plan_i64", "kv8_append", "kv8_attention", "kv8_attention_i64", "kv8_attention_workspace_bytes", "w4_matvec",
             "rsq_qm_build", "rsq_qm_workspace_bytes",
             "rsq_qm_build_fixed_scratch",
             "rsq_status_string",
@@ -445,19 +449,31 @@ def _cache(device_index: int, k_cache, k_scale, v_cache, v_scale):
     return shape
 
 
+def _table_ok(device_index: int, block_table: torch.Tensor) -> bool:
+    """A block table of int32 or int64 ids."""
+    return _lists_ok(device_index, torch.int64 if block_table.dtype is torch.int64 else torch.int32, block_table)
+
+
+def _refuse_table(device_index: int, block_table: torch.Tensor) -> None:
+    """Says what _table_ok found wrong."""
+    if block_table.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"block_table must be int32 or int64, got {block_table.dtype}")
+    _refuse(device_index, block_table.dtype, block_table=block_table)
+
+
 def kv8_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_blocks: torch.Tensor,
              cursor: torch.Tensor, T: int, block_size: int,
              stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """Block tables and slots of a batch of new tokens, on the GPU, from the requests' lengths.
 
-    ctx_len, new_len: int32 B; block_table: int32 B x max_blocks, completed in place with ids
-    free_blocks[cursor], free_blocks[cursor + 1], ... (int32; cursor: int32, one element); T: rows
-    of the (padded) batch.  Returns (cu_new int32 B + 1, seq_len int32 B, positions int32 T,
+    ctx_len, new_len: int32 B; block_table: int32 or int64 B x max_blocks, completed in place with
+    ids free_blocks[cursor], free_blocks[cursor + 1], ... (int32; cursor: int32, one element); T:
+    rows of the (padded) batch.  Returns (cu_new int32 B + 1, seq_len int32 B, positions int32 T,
     slots int64 T, cursor_out int32 1); padding rows get position and slot -1."""
     d = ctx_len.get_device()
-    if d < 0 or not _lists_ok(d, torch.int32, ctx_len, new_len, block_table, free_blocks, cursor):
-        _refuse(d, torch.int32, ctx_len=ctx_len, new_len=new_len, block_table=block_table, free_blocks=free_blocks,
-                cursor=cursor)
+    if d < 0 or not (_lists_ok(d, torch.int32, ctx_len, new_len, free_blocks, cursor) and _table_ok(d, block_table)):
+        _refuse(d, torch.int32, ctx_len=ctx_len, new_len=new_len, free_blocks=free_blocks, cursor=cursor)
+        _refuse_table(d, block_table)
     B = ctx_len.numel()
     if new_len.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B or cursor.numel() != 1:
         raise ValueError("new_len must have B elements, block_table B rows and cursor one element")
@@ -467,10 +483,10 @@ def kv8_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Te
     # one allocation for the int32 results
     cu_new, seq_len, positions, cursor_out = ctx_len.new_empty(2 * B + 2 + T).split_with_sizes((B + 1, B, T, 1))
     slots = ctx_len.new_empty(T, dtype=torch.int64)
-    _check(_lib.kv8_plan(ctx_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(), block_table.shape[1],
-                         block_size, free_blocks.data_ptr(), free_blocks.numel(), cursor.data_ptr(),
-                         cursor_out.data_ptr(), cu_new.data_ptr(), seq_len.data_ptr(), positions.data_ptr(),
-                         slots.data_ptr(), T, _raw_stream(d)))
+    call = _lib.kv8_plan_i64 if block_table.dtype is torch.int64 else _lib.kv8_plan
+    _check(call(ctx_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(), block_table.shape[1], block_size,
+                free_blocks.data_ptr(), free_blocks.numel(), cursor.data_ptr(), cursor_out.data_ptr(), cu_new.data_ptr(),
+                seq_len.data_ptr(), positions.data_ptr(), slots.data_ptr(), T, _raw_stream(d)))
     return cu_new, seq_len, positions, slots, cursor_out
 
 
@@ -516,15 +532,16 @@ def kv8_attention(q: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal attention of the new tokens' queries (T x n_heads*d_h) over the paged 8-bit cache.
 
-    block_table: int32 B x max_blocks, seq_len: int32 B (the new tokens counted), cu_new: int32
+    block_table: int32 or int64 B x max_blocks, seq_len: int32 B (the new tokens counted), cu_new: int32
     B + 1.  sm_scale defaults to 1 / sqrt(d_h).  Rows behind cu_new[B] of out keep their contents.
     workspace: a uint8 CUDA tensor of at least kv8_attention_workspace_bytes(...) (allocated here
     when None).  Returns out (T x n_heads*d_h)."""
     T, width, ldq = _rows(q, "q")
     d = q.get_device()
     n_blocks, n_kv, block_size, d_h = _cache(d, k_cache, k_scale, v_cache, v_scale)
-    if not _lists_ok(d, torch.int32, block_table, seq_len, cu_new):
-        _refuse(d, torch.int32, block_table=block_table, seq_len=seq_len, cu_new=cu_new)
+    if not (_lists_ok(d, torch.int32, seq_len, cu_new) and _table_ok(d, block_table)):
+        _refuse(d, torch.int32, seq_len=seq_len, cu_new=cu_new)
+        _refuse_table(d, block_table)
     B = seq_len.numel()
     if d_h == 0 or width % d_h or block_table.dim() != 2 or block_table.shape[0] != B or cu_new.numel() != B + 1:
         raise ValueError("q must have whole heads, block_table B rows and cu_new B + 1 elements")
@@ -542,11 +559,11 @@ def kv8_attention(q: torch.Tensor, k_cache: torch.Tensor, k_scale: torch.Tensor,
         workspace = k_cache.new_empty(_workspace_bytes(d, T, B, n_heads, n_kv, d_h))
     elif not _lists_ok(d, torch.uint8, workspace):
         _refuse(d, torch.uint8, workspace=workspace)
-    _check(_lib.kv8_attention(q.data_ptr(), ldq, k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(),
-                              v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1], seq_len.data_ptr(),
-                              cu_new.data_ptr(), B, d_h ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), T,
-                              n_heads, n_kv, d_h, block_size, n_blocks, _dtype_code(q), workspace.data_ptr(),
-                              workspace.numel(), _raw_stream(d)))
+    call = _lib.kv8_attention_i64 if block_table.dtype is torch.int64 else _lib.kv8_attention
+    _check(call(q.data_ptr(), ldq, k_cache.data_ptr(), k_scale.data_ptr(), v_cache.data_ptr(), v_scale.data_ptr(),
+                block_table.data_ptr(), block_table.shape[1], seq_len.data_ptr(), cu_new.data_ptr(), B,
+                d_h ** -0.5 if sm_scale is None else sm_scale, out.data_ptr(), T, n_heads, n_kv, d_h, block_size,
+                n_blocks, _dtype_code(q), workspace.data_ptr(), workspace.numel(), _raw_stream(d)))
     return out
 
 
