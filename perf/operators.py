@@ -200,7 +200,7 @@ def prepare(case, seed):
     cols = torch.arange(width, device=DEV, dtype=torch.int32)
     first = torch.cumsum(held, 0) - held
     at = first[:, None] + cols[None]
-    s["table"] = torch.where(cols[None] < held[:, None], order[at.clamp(max=pool - 1).long()], torch.full_like(at, -1)).to(torch.int32)
+    s["table"] = torch.where(cols[None] < held[:, None], order[at.clamp(max=pool - 1).long()], torch.full_like(at, -1))
     if c["op"] == "plan":
         # the ids behind those in use are free; the first two of them went to an earlier call
         taken = int(sum(_blocks(a, size) for a in ctx))
