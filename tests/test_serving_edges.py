@@ -91,3 +91,65 @@ def test_tables_of_other_types_are_refused():
     with pytest.raises(ValueError):
         rsq.kv8_attention(*args, i64(c.table).repeat(1, 2)[:, ::2], i32(c.seq), i32(c.cu))
     assert rsq.launch_count() == before
+
+
+# ---------------------------------------------------------------------------------------------- values that are no numbers
+
+# 256 rows (new tokens x heads of a group) and 2^19 pairs of a row and a token make a request long
+LONG = [(0, 800), (45, 4), (1500, 300)]
+
+
+@pytest.mark.parametrize("size", [16, 32, 64, 128])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_attention_long_chunks_with_bad_values_in_front(dh, size):
+    """A block whose value scale is NaN or infinite reaches every row that sees it, also where it is the first that a row
+    sees, or all that it sees, or the rest of its 128 keys weighs nothing."""
+    for bad in (float("nan"), float("inf")):
+        c = Case(LONG, size, 4, 2, dh, torch.bfloat16, 21)
+        first = [c.table[0][0], c.table[2][0]]
+        c.vs[first] = bad
+        c.check("first block")
+        c.vs[[c.table[b][j] for b in (0, 2) for j in range(1, 128 // size)]] = 0.0
+        c.check("first block, no weight on the rest of the tile")
+        c.vs[[c.table[b][j] for b in (0, 2) for j in range(128 // size)]] = bad
+        c.check("the first 128 tokens")
+        c = Case(LONG, size, 4, 2, dh, torch.bfloat16, 22)
+        c.vs[[j for j in c.table[2] if j >= 0], 0] = bad
+        c.vs[[j for j in c.table[0] if j >= 0], 1] = 0.0
+        c.vs[c.table[0][300 // size], 1] = bad
+        c.check("a head of nothing else, one among zeros")
+
+
+@pytest.mark.parametrize("dh,size", [(64, 128), (128, 16), (128, 128)])
+def test_attention_long_chunks_with_bad_values_in_every_piece(dh, size):
+    """The keys of a few tiles of rows are spread over the GPU in pieces: wherever the poisoned 128 tokens lie, all rows see
+    them."""
+    c = Case([(20000, 130)], size, 4, 1, dh, torch.bfloat16, 23)
+    q, kc, ks, vc = (x.to(DEV) for x in (c.q, c.kc, c.ks, c.vc))
+    table, seq, cu = i32(c.table), i32(c.seq), i32(c.cu)
+    clean = c.vs.to(DEV)
+    outs = []
+    for tile in range(0, 156, 5):
+        vs = clean.clone()
+        vs[c.table[0][tile * 128 // size:(tile + 1) * 128 // size]] = float("nan")
+        outs.append(_rsq().kv8_attention(q, kc, ks, vc, vs, table, seq, cu).isnan().all())
+    assert torch.stack(outs).all(), [5 * i for i, o in enumerate(outs) if not o]
+    assert not _rsq().kv8_attention(q, kc, ks, vc, clean, table, seq, cu).isnan().any()
+
+
+@pytest.mark.parametrize("size", [16, 128])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_attention_long_chunks_with_bad_blocks_anywhere(dh, size):
+    """Poisoned, foreign and missing blocks at the beginning, inside and at the end of requests of many pairs."""
+    for where in (0.0, 0.1, 0.5, 0.9):
+        c = Case(LONG, size, 4, 2, dh, torch.bfloat16, 26)
+        at = [int(where * s) // size for s in c.seq]
+        c.ks[c.table[0][at[0]], 0] = float("nan")
+        c.ks[c.table[2][at[2]], 1] = float("inf")
+        c.vs[c.table[2][at[2]], 0] = float("inf")
+        c.check(f"poisoned at {where}")
+        c = Case(LONG, size, 4, 2, dh, torch.bfloat16, 27)
+        c.table[0][at[0]] = 1 << 30
+        c.table[1][at[1]] = c.n_blocks
+        c.table[2][at[2]] = -1
+        c.check(f"foreign at {where}", want_status=8)

@@ -593,8 +593,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const Kv8Att
 #pragma unroll
                         for (int h = 0; h < HB; ++h) {
                             const float f = qf * __shfl_sync(0xFFFFFFFFu, ks_j, 32 * q / W + h);
-                            const float up = ms - R + __shfl_sync(0xFFFFFFFFu, lv_j, 32 * q / W + h);
-                            const float wb = R == -INFINITY ? 0.f : ex2(up > 120.f ? 120.f : up);
+                            // a value scale that is no number does not raise R, and counts whatever R is
+                            const float lvb = __shfl_sync(0xFFFFFFFFu, lv_j, 32 * q / W + h), up = ms - R + lvb;
+                            const float wb = lvb != lvb ? lvb : R == -INFINITY ? 0.f : ex2(up > 120.f ? 120.f : up);
 #pragma unroll
                             for (int c = HW * h; c < HW * h + HW; c += 2) {
                                 float y[2];
