@@ -153,3 +153,15 @@ def test_attention_long_chunks_with_bad_blocks_anywhere(dh, size):
         c.table[1][at[1]] = c.n_blocks
         c.table[2][at[2]] = -1
         c.check(f"foreign at {where}", want_status=8)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dh", [16, 32, 64, 128])
+def test_attention_bad_values_that_weigh_nothing(dh, dtype):
+    """A NaN value scale counts also where the block's probabilities are below the smallest number."""
+    for size in (16, 64):
+        lens = [(90, 1), (300, 60), (17, 3)] + ([(0, 800)] if dtype == torch.bfloat16 and dh >= 64 else [])
+        c = Case(lens, size, 4, 2, dh, dtype, 24, sharp=400.0)
+        for r in c.table:
+            c.vs[r[0]] = float("nan")
+        c.check(f"size={size}")

@@ -527,7 +527,7 @@ k_kv8_attention_mma(const Kv8Attention p, const Split sp) {
                             float v = ex2(s[n][i][2 * c + e] - base);
                             sum += v;
                             if (p.shift > 4) v *= 32768.f;
-                            else if (v != 0.f) v = v * (i ? xb : xa) * rs;
+                            else if (s[n][i][2 * c + e] != -INFINITY) v = v * (i ? xb : xa) * rs;   // masked: not 0 times a NaN
                             x[e][i][c] = v;
                         }
                     l[n][e] = l[n][e] * co[n][e] + sum * cn[n][e];

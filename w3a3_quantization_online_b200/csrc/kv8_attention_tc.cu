@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const Kv8Att
                                     float x = fmaf(__uint_as_float(v[c + e]), f, -ms);
                                     x = ex2(bits >> (c + e) & 1 ? x : -INFINITY);
                                     sum += x;
-                                    y[e] = x == 0.f ? 0.f : x * wb;
+                                    y[e] = bits >> (c + e) & 1 ? x * wb : 0.f;    // not 0 times a NaN that is masked
                                 }
                                 pk[c >> 1] = pack_f16(y[0], y[1]);
                             }
