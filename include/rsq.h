@@ -301,7 +301,8 @@ int kv8_append(const void *k, int64_t ldk, const void *v, int64_t ldv, const int
  * with scores, softmax and sums in float32, rounded once to `dtype`.  A row that
  * sees no token (p_i < 0) becomes 0; rows from cu_new[B] on are left as they
  * are.  Scales are not negative; a block whose scale is infinite or NaN gives NaN
- * to the rows that see it, and to no other.  out: T x (n_heads * d_h), contiguous.  Blocks may be shared by requests.
+ * to the rows that see it, and to no other, whatever its tokens weigh; a query with an
+ * infinity or NaN makes its own row NaN.  out: T x (n_heads * d_h), contiguous.  Blocks may be shared by requests.
  * workspace: device memory of at least kv8_attention_workspace_bytes(...)
  * bytes (RSQ_ERR_VALUE if smaller), 16-byte aligned; its contents on entry do not
  * matter, and two calls whose work may overlap on the GPU (two streams, two

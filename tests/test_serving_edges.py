@@ -165,3 +165,22 @@ def test_attention_bad_values_that_weigh_nothing(dh, dtype):
         for r in c.table:
             c.vs[r[0]] = float("nan")
         c.check(f"size={size}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dh", [16, 64, 128])
+def test_attention_of_queries_that_are_no_numbers(dh, dtype):
+    """An infinity in a query makes every score infinite or NaN and the row NaN, also where all of them are -infinity, and no
+    other row.  (The others keep to the references' tolerance, not to the bits without it: 32 rows of a long chunk take the
+    products of probabilities and value scales in one way or the other together, each within that tolerance.)"""
+    for size in (16, 64):
+        lens = [(0, 1), (40, 1), (0, 20), (300, 60)] + ([(0, 800)] if dtype == torch.bfloat16 and dh >= 64 else [])
+        c = Case(lens, size, 4, 2, dh, dtype, 25)
+        c.kc[..., 5] = -c.kc[..., 5].abs().clamp(min=1)     # no zero code meets the infinity
+        head = torch.arange(4) * dh + 5
+        rows = list(range(0, len(c.q), 3))
+        c.q[rows[0::3], head[1]] = float("inf")
+        c.q[rows[1::3], head[1]] = float("-inf")
+        c.q[rows[2::3], head[1]] = float("nan")
+        assert c.run().reshape(-1, 4, dh)[rows, 1].isnan().all()
+        c.check(f"size={size}")

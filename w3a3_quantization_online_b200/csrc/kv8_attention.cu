@@ -59,8 +59,9 @@ __global__ void __launch_bounds__(kGenWarps * 32) k_kv8_attention_any(const Kv8A
     float o[16], qs[16];
 #pragma unroll
     for (int e = 0; e < 16; e += 8) load8(q + sub * 16 + e, *reinterpret_cast<float(*)[8]>(&qs[e]));
+    // an infinity makes every score of the row infinite or NaN: a row whose scores are all -infinity is NaN too
 #pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+    for (int e = 0; e < 16; ++e) qs[e] = fabsf(qs[e]) < INFINITY ? qs[e] : NAN, o[e] = 0.f;
     float m = -INFINITY, l = 0.f;
     for (int key0 = warp * 32; key0 < seen; key0 += kGenWarps * 32) {
         const int key = key0 + lane;

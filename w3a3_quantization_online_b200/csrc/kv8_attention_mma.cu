@@ -413,7 +413,8 @@ k_kv8_attention_mma(const Kv8Attention p, const Split sp) {
             most = max_t(most);
             // 2^(14 - exponent), from the bits; rows below 2^-100 keep that factor
             const int ex = max(int(__float_as_uint(most) >> 23) - 127, -100);
-            const float up = __uint_as_float(uint32_t(127 + min(14 - ex, 114)) << 23);
+            // an infinity makes every score of the row infinite or NaN: a row whose scores are all -infinity is NaN too
+            const float up = most < INFINITY ? __uint_as_float(uint32_t(127 + min(14 - ex, 114)) << 23) : NAN;
             const float f = __uint_as_float(uint32_t(127 - min(14 - ex, 114)) << 23) * (p.sm_scale * kLog2e);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {

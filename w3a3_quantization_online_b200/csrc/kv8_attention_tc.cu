@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const Kv8Att
                         if (lane / RI == c0 + c) ex = own;
                         float sg = __uint_as_float(uint32_t(127 + up) << 23);
                         if (p.sm_scale < 0.f) sg = -sg;            // the sign goes with q: factors stay positive
+                        if (most >= 0x7F80u) sg = NAN;             // an infinity too: every score is infinite or NaN
                         uint32_t h[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
