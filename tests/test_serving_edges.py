@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import serving_ref as R
-from tests.test_serving import DEV, Case, _rsq, i32
+from tests.test_serving import DEV, Case, _rsq, gen, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -184,3 +184,34 @@ def test_attention_of_queries_that_are_no_numbers(dh, dtype):
         c.q[rows[2::3], head[1]] = float("nan")
         assert c.run().reshape(-1, 4, dh)[rows, 1].isnan().all()
         c.check(f"size={size}")
+
+
+# ---------------------------------------------------------------------------------------------- 4-bit weights
+
+@pytest.mark.parametrize("group", [32, 64, 96, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_matvec_keeps_infinities(dtype, group):
+    """An infinity in x gives an infinity of the formula's sign, NaN where it meets a code of 0 or another sign; NaN gives NaN,
+    whichever bits of its payload are set."""
+    rsq = _rsq()
+    g = gen(group)
+    for T in (1, 3, 6, 8, 9, 20, 24, 25, 33, 48, 64, 70):
+        N, K = 150, 4 * group
+        x = torch.randn((T, K), generator=g).to(dtype)
+        x[0, 17] = float("inf")
+        x[T // 2, K - 3] = float("-inf")
+        if T > 4:
+            x[T - 1, 40], x[T - 1, 2] = float("inf"), float("-inf")
+            x[1, 33] = float("nan")
+            if dtype == torch.float32:
+                x.view(torch.int32)[2, 9] = 0x7F800001      # a NaN whose upper half is that of an infinity
+        codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+        scales = torch.exp(torch.randn((N, K // group), generator=g)) * 0.01
+        want, big = R.matvec(x, codes, scales)
+        got = rsq.w4_matvec(x.to(DEV), codes.to(DEV), scales.to(DEV), out_dtype=torch.float32).cpu().double()
+        assert torch.equal(got.isnan(), want.isnan()), f"T={T}: NaN in other places"
+        inf = want.isinf()
+        assert inf.any() and torch.equal(got.isinf(), inf) and torch.equal(got[inf], want[inf]), f"T={T}"
+        fine = want.isfinite()
+        tol = R.matvec_tol(want, big, K, torch.float32)
+        assert ((got - want).abs()[fine] <= tol[fine]).all(), f"T={T}"

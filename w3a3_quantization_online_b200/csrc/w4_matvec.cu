@@ -171,8 +171,11 @@ __global__ void __launch_bounds__(kMvThreads) k_w4_matvec(const MatvecArgs p, in
         for (int j = 0; j < C::kLoads; ++j) {
             const int i = tid + j * kMvThreads, t = i / (C::KC / 4), k4 = i % (C::KC / 4);
             if (t >= C::TT) continue;
-            float r[4] = {ahead[j].x, ahead[j].y, ahead[j].z, ahead[j].w};
-            // parts cut off, not rounded: exact, and no finite value becomes an infinity
+            // (adding 0 sets the upper bits of every NaN)
+            float r[4] = {__fadd_rn(ahead[j].x, 0.f), __fadd_rn(ahead[j].y, 0.f), __fadd_rn(ahead[j].z, 0.f),
+                          __fadd_rn(ahead[j].w, 0.f)};
+            // parts cut off, not rounded: exact, and no finite value becomes an infinity; the lower parts of an
+            // infinity are NaN, and left out when the parts are joined
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
                 const int row = q * C::TT + t;
@@ -315,12 +318,17 @@ __global__ void __launch_bounds__(kMvThreads) k_w4_matvec(const MatvecArgs p, in
         if (tok < p.T && n < p.N) static_cast<typename OUT::T *>(p.y)[tok * p.N + n] = OUT::from_f(v);
     };
     for (int i = tid; i < kOut; i += kMvThreads) {
-        // the parts of a float32 x from the smallest one up
-        float v = 0.f;
+        // the parts of a float32 x from the smallest one up; where x has an infinity or NaN, the first part says all
+        float v = 0.f, first = 0.f;
 #pragma unroll
         for (int q = kParts - 1; q >= 0; --q)
 #pragma unroll
-            for (int w = 0; w < C::KW; ++w) v += s_y[w * kAll + q * kOut + i];
+            for (int w = 0; w < C::KW; ++w) {
+                const float part = s_y[w * kAll + q * kOut + i];
+                v += part;
+                if (q == 0) first += part;
+            }
+        if (kParts > 1 && !(fabsf(first) < __int_as_float(0x7F800000))) v = first;
         if (ks == 1) put(i, v);
         else s_y[i] = v;
     }

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kTcThreads, (MvTcCfg<IO, NX, G32>::kMin)) k_w4
 #pragma unroll
                     for (int e = 0; e < 8; ++e) r[e] = 0.f;
                 }
-                // parts cut off, not rounded: exact, and no finite value becomes an infinity
+                // parts cut off, not rounded: exact, and no finite value becomes an infinity; nothing is left of an infinity
 #pragma unroll
                 for (int q = 0; q < 3; ++q) {
                     const int row = q * TT + t;
@@ -208,7 +208,10 @@ __global__ void __launch_bounds__(kTcThreads, (MvTcCfg<IO, NX, G32>::kMin)) k_w4
                     for (int e = 0; e < 4; ++e) h[e] = prmt(__float_as_uint(r[2 * e]), __float_as_uint(r[2 * e + 1]), 0x7632u);
                     *reinterpret_cast<uint4 *>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) r[e] -= __uint_as_float(__float_as_uint(r[e]) & 0xFFFF0000u);
+                    for (int e = 0; e < 8; ++e) {
+                        const float left = r[e] - __uint_as_float(__float_as_uint(r[e]) & 0xFFFF0000u);
+                        r[e] = q == 0 && fabsf(r[e]) == __int_as_float(0x7F800000) ? 0.f : left;
+                    }
                 }
             }
         }
