@@ -141,7 +141,7 @@ struct Kv8Attention {
     int B, n_heads, n_kv, dh, shift, width;
     long long n_blocks;
     float sm_scale;
-    bool wide_table;
+    int wide_table;    // 1: int64
 };
 // Head sizes without a tensor-core kernel, and any other (CUDA cores, float32).
 cudaError_t launch_kv8_attention_any(const Kv8Attention &p, int dtype, cudaStream_t s);

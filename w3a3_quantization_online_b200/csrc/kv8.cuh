@@ -31,11 +31,11 @@ __device__ __forceinline__ float kv8_scale(float v) {
     return fabsf(v) < __int_as_float(0x7F800000) ? v : __int_as_float(0x7FC00000);
 }
 
-// Entry i of the block table; an int64 one outside the cache reads as -1.
+// Entry i of the block table; -1 for an int64 one that is more than its lower half.
 __device__ __forceinline__ int kv8_block(const Kv8Attention &p, long long i) {
-    if (!p.wide_table) return static_cast<const int32_t *>(p.table)[i];
-    const long long id = static_cast<const int64_t *>(p.table)[i];
-    return id >= 0 && id < p.n_blocks ? int(id) : -1;
+    const int32_t *at = static_cast<const int32_t *>(p.table) + (i << p.wide_table);
+    const int id = at[0], above = p.wide_table ? at[1] : 0;
+    return above ? -1 : id;
 }
 
 // The part of a request's state that every kernel clamps the same way: `n` new
