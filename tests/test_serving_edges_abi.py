@@ -1,4 +1,8 @@
-"""Host-side refusals of the serving entry points with int64 block tables."""
+"""Host side of the serving entry points beside test_serving_abi.py: refusals with int64 block tables, the binding's import."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -39,3 +43,16 @@ def test_valid_calls_reach_the_launch():
         pytest.skip("would launch on fake pointers")
     assert _plan() == CUDA and _plan(seq=A[2] + 4 * 8 * 8) == CUDA
     assert _attend() == CUDA and _attend(ws=A[5] + 4 * 8 * 8) == CUDA
+
+
+def test_binding_imports_without_torchs_short_cuts():
+    """Builds of torch without CUDA lack them; where only they are gone, the public calls answer instead."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "from w3a3_quantization_online_b200 import rsq\n"
+            "torch.cuda.current_stream = lambda d: type('S', (), {'cuda_stream': 40 + d})\n"
+            "assert rsq._raw_stream(2) == 42 and rsq._current_device is torch.cuda.current_device\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr

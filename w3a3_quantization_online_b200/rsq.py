@@ -400,8 +400,11 @@ def _enter(device_index: int, stream):
     return torch.cuda.stream(stream)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# The current stream's handle and the current device, by torch's own short cuts where this torch has them: a few
+# microseconds less per call than the public ones.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device_index: torch.cuda.current_stream(device_index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _lists_ok(device_index: int, dtype, *tensors: torch.Tensor) -> bool:
