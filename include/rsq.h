@@ -328,7 +328,9 @@ uint64_t kv8_attention_workspace_bytes(int64_t T, int B, int n_heads, int n_kv, 
  * takes them as they are (T x K `dtype`, rows ldx elements apart).  codes_w: N
  * rows of K/2 bytes, packed as for w4a4_gemm (any 4-bit two's complement
  * value); scales_w: N x (K / group) float32.  y: T x N, contiguous, rounded once
- * to out_dtype (RSQ_F32, RSQ_BF16 or RSQ_F16) from float32 sums.  Any N up to
+ * to out_dtype (RSQ_F32, RSQ_BF16 or RSQ_F16) from float32 sums.  Scales are finite, and
+ * meet sums of x * code over up to 64 inputs: those have to stay finite in float32, which |x| < 2^118
+ * always does.  An infinity or NaN in x reaches its own row only.  Any N up to
  * 2^20; group a multiple of 32 that divides K <= 2^20 (group = K: one scale per
  * output); T <= 65536 (meant for up to a few dozen rows: the weights are read
  * again for every 64). */

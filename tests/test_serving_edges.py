@@ -215,3 +215,20 @@ def test_matvec_keeps_infinities(dtype, group):
         fine = want.isfinite()
         tol = R.matvec_tol(want, big, K, torch.float32)
         assert ((got - want).abs()[fine] <= tol[fine]).all(), f"T={T}"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_matvec_of_the_largest_x_there_may_be(dtype):
+    """|x| < 2^118: the products of a group with the codes stay finite before they meet its scale."""
+    rsq = _rsq()
+    for group in (32, 128):
+        for T in (2, 7, 30, 66):
+            x = torch.full((T, 256), 2.0 ** 118).to(dtype)
+            x[:, ::2] *= 1 - torch.finfo(dtype).eps / 2      # the largest below it
+            x[:, 1::2] = x[:, ::2]
+            x[1] = -x[1]
+            codes = torch.full((20, 128), 0x88, dtype=torch.uint8)      # -8
+            scales = torch.full((20, 256 // group), 2.0 ** -30)
+            want, big = R.matvec(x, codes, scales)
+            got = rsq.w4_matvec(x.to(DEV), codes.to(DEV), scales.to(DEV), out_dtype=torch.float32).cpu().double()
+            assert ((got - want).abs() <= R.matvec_tol(want, big, 256, torch.float32)).all()
