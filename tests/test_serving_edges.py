@@ -186,6 +186,15 @@ def test_attention_of_queries_that_are_no_numbers(dh, dtype):
         c.check(f"size={size}")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dh", [16, 32, 256])
+def test_attention_several_tokens_of_other_head_sizes(dh, dtype):
+    for i, (H, kv) in enumerate([(1, 1), (8, 2), (5, 1), (32, 2)]):
+        size = (16, 32, 64, 128)[i]
+        lens = [(0, 2), (40, 3), (0, 0), (size - 1, 2), (100, 17), (size, 5), (0, 33), (3, 140)]
+        Case(lens, size, H, kv, dh, dtype, 28 + i, pad=2, strided=i % 2 == 1).check(f"H={H} kv={kv}")
+
+
 # ---------------------------------------------------------------------------------------------- 4-bit weights
 
 @pytest.mark.parametrize("group", [32, 64, 96, 128])
@@ -232,3 +241,19 @@ def test_matvec_of_the_largest_x_there_may_be(dtype):
             want, big = R.matvec(x, codes, scales)
             got = rsq.w4_matvec(x.to(DEV), codes.to(DEV), scales.to(DEV), out_dtype=torch.float32).cpu().double()
             assert ((got - want).abs() <= R.matvec_tol(want, big, 256, torch.float32)).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("group", [32, 64, 96])
+def test_matvec_is_exact_on_whole_numbers_for_any_rows(group, dtype):
+    """Whole x and scales of powers of two: every sum is exact, in both kernels and their variants."""
+    rsq = _rsq()
+    g = gen(group)
+    for T in (1, 6, 9, 17, 24, 30, 33, 48, 64, 70):
+        K = group * 9
+        x = torch.randint(-8, 9, (T, K), generator=g).to(dtype)
+        codes = torch.randint(0, 256, (140, K // 2), generator=g, dtype=torch.uint8)
+        scales = 2.0 ** torch.randint(-2, 3, (140, 9), generator=g).float()
+        want, _ = R.matvec(x, codes, scales)
+        got = rsq.w4_matvec(x.to(DEV), codes.to(DEV), scales.to(DEV), out_dtype=torch.float32)
+        assert torch.equal(got.cpu().double(), want), f"T={T}"
