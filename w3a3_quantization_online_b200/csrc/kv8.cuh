@@ -37,6 +37,13 @@ __device__ __forceinline__ int kv8_block(const Kv8Attention &p, long long i) {
     const int id = at[0], above = p.wide_table ? at[1] : 0;
     return above ? -1 : id;
 }
+// The same where the table's type is known.
+template <bool kWide>
+__device__ __forceinline__ int kv8_block(const Kv8Attention &p, long long i) {
+    if (!kWide) return static_cast<const int32_t *>(p.table)[i];
+    const int2 id = static_cast<const int2 *>(p.table)[i];
+    return id.y ? -1 : id.x;
+}
 
 // The part of a request's state that every kernel clamps the same way: `n` new
 // rows starting at row `first` of the T token rows, `pos0` the position of the

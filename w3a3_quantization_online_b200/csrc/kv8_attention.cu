@@ -11,6 +11,10 @@
 // tile of 32 keys, 16 columns of a key to a lane, all in float32, and are joined through
 // shared memory.  It is bound by instructions (a conversion and an fma for each code and query
 // head: the heads of a group do not share them) and, for one long request, by the warps there are.
+// Two CTAs to an SM, that is 64 registers a thread, are worth more than the few that then spill: d_h 32 68 and 103 us, d_h 256
+// 281 and 352 us with 78.  For d_h 256 the compiler is left to find them (281 us; 323 with the bound written down, as it
+// then keeps fewer loads on the way), which it does as long as little else lives through the loop: so the type of
+// the block table is a template argument, and the check of the query touches one of its columns.
 // Measured: 61 requests of up to 8192 tokens, 32 query over 8 key heads, d_h 32 68 us, d_h 256
 // 282 us (4 warps: 102 and 801; a key to a lane for the scores and a few columns to a lane
 // for the values, the codes loaded byte by byte: 890 and 1509).
@@ -31,8 +35,8 @@ __device__ __forceinline__ void codes16(const uint4 &u, float (&f)[16]) {
         f[i] = __uint_as_float(prmt(w[i >> 2], 0x4B000000u, 0x7650u | uint32_t(i & 3))) - 8388736.f;
 }
 
-template <class IO, int dh>
-__global__ void __launch_bounds__(kGenWarps * 32) k_kv8_attention_any(const Kv8Attention p) {
+template <class IO, int dh, bool kWide>
+__global__ void __launch_bounds__(kGenWarps * 32, dh == 256 ? 0 : 2) k_kv8_attention_any(const Kv8Attention p) {
     using T = typename IO::T;
     __shared__ float s_o[kGenWarps][dh];
     __shared__ float s_m[kGenWarps], s_l[kGenWarps];
@@ -60,15 +64,17 @@ __global__ void __launch_bounds__(kGenWarps * 32) k_kv8_attention_any(const Kv8A
 #pragma unroll
     for (int e = 0; e < 16; e += 8) load8(q + sub * 16 + e, *reinterpret_cast<float(*)[8]>(&qs[e]));
     // an infinity makes every score of the row infinite or NaN: a row whose scores are all -infinity is NaN too
+    float most = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) qs[e] = fabsf(qs[e]) < INFINITY ? qs[e] : NAN, o[e] = 0.f;
+    for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(qs[e])), o[e] = 0.f;
+    qs[0] += most < INFINITY ? 0.f : NAN;
     float m = -INFINITY, l = 0.f;
     for (int key0 = warp * 32; key0 < seen; key0 += kGenWarps * 32) {
         const int key = key0 + lane;
         bool vis = key < seen;
         long long row = 0, at = 0;                 // (block, head) of this lane's key, its first code
         if (vis) {
-            const int id = kv8_block(p, (long long)lo * p.width + (key >> p.shift));
+            const int id = kv8_block<kWide>(p, (long long)lo * p.width + (key >> p.shift));
             vis = id >= 0 && id < p.n_blocks;
             if (!vis) kv8_report(p.status, kErrKvBlock);
             else row = (long long)id * p.n_kv + kvh, at = ((row << p.shift) + (key & (S - 1))) * dh;
@@ -138,19 +144,25 @@ __global__ void __launch_bounds__(kGenWarps * 32) k_kv8_attention_any(const Kv8A
     }
 }
 
-template <class IO>
+template <class IO, int dh>
 void launch(const Kv8Attention &p, dim3 grid, cudaStream_t s) {
-    if (p.dh == 16) k_kv8_attention_any<IO, 16><<<grid, kGenWarps * 32, 0, s>>>(p);
-    else if (p.dh == 32) k_kv8_attention_any<IO, 32><<<grid, kGenWarps * 32, 0, s>>>(p);
-    else k_kv8_attention_any<IO, 256><<<grid, kGenWarps * 32, 0, s>>>(p);
+    if (p.wide_table) k_kv8_attention_any<IO, dh, true><<<grid, kGenWarps * 32, 0, s>>>(p);
+    else k_kv8_attention_any<IO, dh, false><<<grid, kGenWarps * 32, 0, s>>>(p);
+}
+
+template <class IO>
+void launch_dh(const Kv8Attention &p, dim3 grid, cudaStream_t s) {
+    if (p.dh == 16) launch<IO, 16>(p, grid, s);
+    else if (p.dh == 32) launch<IO, 32>(p, grid, s);
+    else launch<IO, 256>(p, grid, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_attention_any(const Kv8Attention &p, int dtype, cudaStream_t s) {
     const dim3 grid(unsigned(p.T), unsigned(p.n_heads));
-    if (dtype == 0) launch<F32>(p, grid, s);
-    else launch<BF16>(p, grid, s);
+    if (dtype == 0) launch_dh<F32>(p, grid, s);
+    else launch_dh<BF16>(p, grid, s);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(1);
     return e;
