@@ -37,7 +37,11 @@ __device__ __forceinline__ int kv8_block(const Kv8Attention &p, long long i) {
     const int id = at[0], above = p.wide_table ? at[1] : 0;
     return above ? -1 : id;
 }
-// The same where the table's type is known.
+// Its lower half alone, for where any block may be read in place of one that is none.
+__device__ __forceinline__ int kv8_block_low(const Kv8Attention &p, long long i) {
+    return static_cast<const int32_t *>(p.table)[i << p.wide_table];
+}
+// Entry i where the table's type is known.
 template <bool kWide>
 __device__ __forceinline__ int kv8_block(const Kv8Attention &p, long long i) {
     if (!kWide) return static_cast<const int32_t *>(p.table)[i];

@@ -758,9 +758,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const Kv8Att
             const Piece it = piece_at(at);
             if (it.none) continue;
             // lane r < 16: the cache row of keys 8 r of a tile; the table is read a tile ahead
+            // (the lower half of an int64 id will do: the softmax masks what is no block; both halves took 527 us
+            // where this takes 521)
             auto id_at = [&](int j) -> int {
                 const int key = j * 128 + (lane & 15) * 8;
-                return key < it.kend ? kv8_block(p, (long long)it.b * p.width + (key >> p.shift)) : 0;
+                return key < it.kend ? kv8_block_low(p, (long long)it.b * p.width + (key >> p.shift)) : 0;
             };
             const int in_block = ((lane & 15) * 8) & ((1 << p.shift) - 1);
             long long row = 0;
