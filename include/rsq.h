@@ -298,7 +298,13 @@ int kv8_append(const void *k, int64_t ldk, const void *v, int64_t ldv, const int
  * sees the tokens at positions 0 .. p_i; query head h reads key head
  * h / (n_heads / n_kv):
  *     s_j = sm_scale * <q, k_j>,  out = sum_j softmax(s)_j v_j
- * with scores, softmax and sums in float32, rounded once to `dtype`.  A row that
+ * with scores, softmax statistics and sums in float32, rounded once to `dtype`.
+ * On the way, for d_h 64 and 128: the codes are exact; an element of q enters the
+ * products exactly (bf16) or within 2^-23 of itself (float32), or within 2^-39 of its
+ * row's largest element, whichever is more; a probability meets the values within 2^-11 of
+ * itself (bf16) or 2^-23 (float32), or within 2^-37 of the row's largest product of a
+ * probability and its value scale.  The other d_h take both in float32.  Exponentials are
+ * the GPU's own (about 2^-22 relative); float32 alone does not mean float32 results bit by bit.  A row that
  * sees no token (p_i < 0) becomes 0; rows from cu_new[B] on are left as they
  * are.  Scales are not negative; a block whose scale is infinite or NaN gives NaN
  * to the rows that see it, and to no other, whatever its tokens weigh; a query with an

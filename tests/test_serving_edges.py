@@ -195,6 +195,36 @@ def test_attention_several_tokens_of_other_head_sizes(dh, dtype):
         Case(lens, size, H, kv, dh, dtype, 28 + i, pad=2, strided=i % 2 == 1).check(f"H={H} kv={kv}")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_attention_of_a_query_element_far_above_the_rest(dh, dtype):
+    """The largest element of a row is 2^32 times the rest and meets only codes of 0.  Each of the others is off by up to
+    2^-39 of it, so a score by E = |sm_scale| 2^-39 max |q| sum |k| and a probability by exp(E) - 1 of itself; the output by
+    that twice (numerator and denominator) times A."""
+    for size in (16, 64):
+        lens = [(300, 1), (40, 70)] + ([(0, 800)] if dtype == torch.bfloat16 else [])
+        c = Case(lens, size, 4, 2, dh, dtype, 31)
+        c.kc[..., 7] = 0
+        c.q.reshape(-1, 4, dh)[..., 7] = 2.0 ** 32
+        got = c.run().cpu().double().reshape(-1, 4, dh)
+        want, big, S = R.attention(c.q, c.kc, c.ks, c.vc, c.vs, c.table, c.seq, c.cu, c.sm)
+        keys = (c.kc.double().abs().sum(-1) * c.ks.double()[..., None]).amax()
+        E = c.sm * 2.0 ** -39 * 2.0 ** 32 * keys
+        assert E < 0.5
+        tol = R.attention_tol(want, big, S, max(c.seq), dh, dtype) + 2 * torch.expm1(E) * big
+        assert ((got - want).abs() <= tol).all(), f"size={size}"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dh", [32, 64, 128])
+def test_attention_without_a_scale_of_scores(dh, dtype):
+    """sm_scale 0: the mean of what a row sees."""
+    for size in (16, 64):
+        c = Case([(0, 1), (77, 3), (0, 800)], size, 2, 2, dh, dtype, 32)
+        c.sm = 0.0
+        c.check(f"size={size}")
+
+
 # ---------------------------------------------------------------------------------------------- 4-bit weights
 
 @pytest.mark.parametrize("group", [32, 64, 96, 128])

@@ -25,11 +25,12 @@
 //     bytes of its keys; V: the order of the output columns is free, so a lane
 //     takes 16 (8) consecutive bytes of four keys and pairs them bytewise;
 //   * q is scaled by a power of two per row so that its largest value lies in
-//     [2^14, 2^15): a bf16 q is then exact in fp16 (down to 2^-38 of the largest),
-//     a float32 q is taken as the sum of two fp16 parts (22 bits and a sign);
+//     [2^14, 2^15): a bf16 q is then exact in fp16 down to 2^-31 of the largest,
+//     a float32 q is taken as the sum of two fp16 parts (22 bits and a sign down to 2^-17);
+//     what is smaller is off by at most half of fp16's smallest step, 2^-39 of the largest;
 //   * probabilities go in relative to their 32 keys' maximum, times 2^15: fp16
-//     keeps 11 bits of them down to 2^-29 (2^-12 relative: a sixteenth of what
-//     rounding the output to bf16 costs); for float32, two fp16 parts.  They are
+//     keeps 11 bits of them down to 2^-29 (off by 2^-11 of itself at most: an eighth of what
+//     rounding the output to bf16 costs); for float32, two fp16 parts (2^-23).  They are
 //     transposed from the first product's layout to the second's by movmatrix;
 //   * every 32 keys are accumulated from zero and join the float32 O with one
 //     multiply and one fma, which carry the change of the maximum and v_scale.

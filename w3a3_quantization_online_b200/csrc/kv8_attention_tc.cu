@@ -24,14 +24,14 @@
 //     and V tiles in the SWIZZLE_128B layout that both products read.  A code
 //     is converted once for 256 rows.
 // q is scaled by a power of two per row so that its largest value lies in
-// [2^14, 2^15): exact in fp16 (down to 2^-38 of the largest).  k_scale joins the scores
-// after the product.  v_scale belongs to a block of keys, so it has to join P: with m
+// [2^14, 2^15): exact in fp16 down to 2^-31 of the largest, below that off by at most half of fp16's smallest
+// step, 2^-39 of the largest.  k_scale joins the scores after the product.  v_scale belongs to a block of keys, so it has to join P: with m
 // the running maximum of the scores and R a reference per row,
 //     x = 2^(s - m) (float32, summed into l),  P = x 2^(m - R + log2 v_scale),
 // R kept within 15 of the largest s + log2 v_scale so far and put 12 below it when
 // that is passed: O is then scaled down in TMEM, which happens a few times per row.
 // The largest P so far lies in [2^12, 2^15]: fp16 keeps 11 bits of all that are above
-// 2^-26 of it (2^-12 relative: a sixteenth of what rounding the output to bf16 costs).
+// 2^-26 of it (off by 2^-11 of itself at most: an eighth of what rounding the output to bf16 costs).
 // Every mbarrier wait is bounded; a timeout sets a bit in the device status
 // word, no more products are issued, and the CTA drains before freeing TMEM.
 #include <type_traits>

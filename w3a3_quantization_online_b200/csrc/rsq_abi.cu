@@ -191,7 +191,10 @@ Span rows_span(const void *p, int64_t T, int64_t ld, int64_t width, int dtype) {
 bool kv8_heads(int n_heads, int n_kv) { return n_heads >= n_kv && n_heads <= 1024 && n_heads % n_kv == 0; }
 
 // Whether a bf16 batch may hold a long request (its lengths lie on the device), for the tcgen05 kernel, where 256
-// rows read the cache together.  A batch of about one token a request is not searched for one.
+// rows read the cache together.  A batch of fewer than two tokens a request on average is not searched for one (the search
+// and the kernels that find nothing cost a decode step some microseconds), so one chunk among many single tokens
+// stays on mma.sync: 256 tokens on 8000 older ones take 202 us with 254 single tokens and 495 us with 300 (alone 75 us; the
+// single tokens alone 118 and 137 us).
 bool kv8_long_chunks(int64_t T, int B, int n_heads, int n_kv) {
     return T * (n_heads / n_kv) >= rsq::kKv8TcRows && T >= 2ll * B;
 }
@@ -614,8 +617,9 @@ int w4_matvec(const void *x, int64_t ldx, const uint8_t *codes_w, const float *s
                         span(scales_w, uint64_t(N) * (K / group) * 4)};
     const Span out[1] = {span(y, uint64_t(T) * N * (out_dtype == RSQ_F32 ? 4 : 2))};
     if (any_overlap(in, out)) return RSQ_ERR_ALIAS;
-    // Measured on tcgen05 and mma.sync: bf16, 8192 x 8192, 48 rows 34 and 51 us, 24 rows 36 and 36 us, 4096 x 4096, 16
-    // rows 14 and 9.4 us; float32, 4096 x 12288, 16 rows 37 and 59 us, 5 rows 34 and 22 us.
+    // Measured on mma.sync and tcgen05 (us): bf16, 8192 x 8192 in groups of 32, 24 rows 32 and 34, 25 rows 57 and 35, 48 rows
+    // 57 and 39; in groups of 128, 24 rows 28 and 35, 48 rows 50 and 33; 4096 x 4096 in groups of 128, 24 rows 11 and 17;
+    // float32, 4096 x 12288 in groups of 64, 8 rows 24 and 38, 9 rows 43 and 38.
     const auto launch = T > (dtype == RSQ_F32 ? 8 : 24) ? rsq::launch_w4_matvec_tc : rsq::launch_w4_matvec;
     return finish(launch(x, ldx, codes_w, scales_w, y, T, N, K, group, dtype, out_dtype,
                          static_cast<cudaStream_t>(stream)));
