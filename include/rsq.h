@@ -339,7 +339,7 @@ uint64_t kv8_attention_workspace_bytes(int64_t T, int B, int n_heads, int n_kv, 
  * always does.  An infinity or NaN in x reaches its own row only.  Any N up to
  * 2^20; group a multiple of 32 that divides K <= 2^20 (group = K: one scale per
  * output); T <= 65536 (meant for up to a few dozen rows: the weights are read
- * again for every 64). */
+ * and unpacked again for every 64, or 16 to 64 float32 ones). */
 int w4_matvec(const void *x, int64_t ldx, const uint8_t *codes_w, const float *scales_w, void *y, int64_t T, int N, int K,
               int group, int dtype, int out_dtype, void *stream);
 

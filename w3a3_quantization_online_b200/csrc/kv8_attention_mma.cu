@@ -38,7 +38,7 @@
 // registers are done, so about 6 KB per warp are on the way.
 //
 // Measured (32 query over 8 key heads of 128, bf16): two requests of up to 131072 tokens, 269 MB,
-// 64 us (4.2 TB/s; the key loops run at about 6 TB/s); 61 requests of up to 8192 tokens, 95 MB, 36 us;
+// 65 us (4.1 TB/s; the key loops run at about 6 TB/s); 61 requests of up to 8192 tokens, 95 MB, 36.5 us;
 // one request of 200 tokens, 32 heads, 11.5 us.  34 float32 tokens of 17 requests, 20 over 4 heads of 64: 16 to 18 us.
 // What is not key loops is finding the range, loading queries and joining.
 #include "kv8.cuh"

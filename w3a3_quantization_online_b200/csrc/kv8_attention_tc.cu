@@ -10,10 +10,12 @@
 // gets the same share of the (item, 128 keys) units, in order, an item counting six units
 // more than it has; an item that is cut leaves its pieces (output, maximum and sum of each row)
 // in the workspace, and a second kernel puts them together in their order.
-// (With whole items, taken from a counter, the last ones ran alone: 562 us where this takes
-// 504, for 4312 new tokens of three requests on up to 5952 older ones, 32 heads over 8 of keys,
-// d_h 128: 784 TFLOP/s.  Repeated for seconds the GPU reaches its 1000 W and takes 557 us.  256 rows by 128 keys take 4400 to 4600 clocks, two thirds of it the
-// softmax of a tile (3000) and the products behind it one after the other.)
+// (With whole items, taken from a counter, the last ones ran alone: 562 us where this took
+// 504 to 519, for 4312 new tokens of three requests on up to 5952 older ones, 32 heads over 8 of keys,
+// d_h 128: 762 TFLOP/s.  Repeated for seconds the GPU reaches its 1000 W and takes 555 us.  256 rows by 128 keys
+// take 4400 to 4600 clocks, two thirds of it the softmax of a tile (3000) and the products behind it one after the
+// other.  Without older tokens an item has 1 to 16 tiles beside its six: 25321 tokens of 20 requests take 731 us,
+// 0.24 of the tensor core's rate.)
 //   * Warps 0-3 and 4-7, a thread to a row: read the scores S (fp32, TMEM) of 128
 //     keys, find the maximum, form the probabilities and put them back into the same
 //     TMEM columns as fp16, where they are the A operand of the next product.

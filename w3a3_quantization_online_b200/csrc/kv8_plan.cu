@@ -12,7 +12,7 @@
 // another, and then serves its share of requests and rows.  A row whose block
 // is a fresh one reads its id from the free list, not from the table that
 // another CTA may still be writing.  The call is a few microseconds of latency
-// whatever its size: 2.8 us for a decode step of 64 requests (2 KB), 3.1 us for 27648
+// whatever its size: 3.0 us for a decode step of 64 requests (2 KB), 3.3 us for 27648
 // rows of 48 prompts (0.35 MB).
 #include "kv8.cuh"
 
